@@ -482,6 +482,7 @@ __device__ __forceinline__ u64 select(Shared<CS>& sh, int n, u64 target, int bit
       __syncthreads();
       return key;
     }
+    __syncthreads();   // every warp has read n_list, which the next turn sets to 0
     if (first < 0) {
       first = b;
     } else {

@@ -252,3 +252,23 @@ def test_finished_rows_repeat_bit_for_bit():
     for _ in range(20):
         again = run(x, u, **kw)
         assert (again[0] == first[0]).all() and (again[1] == first[1]).all()
+
+
+def test_digits_with_more_ties_than_a_list_holds():
+    """Cuts and draws among 1600 equal logits side by side: every selection is split by the keys' bits, by 128 and
+    more keys a digit, in each of the three selections of a row, again and again."""
+    R, V, n = 96, 262144, 1600
+    at = np.random.RandomState(8).randint(0, V - n, R)
+    x = torch.full((R, V), -30.0, device="cuda")
+    for r in range(R):
+        x[r, at[r]:at[r] + n] = 2.0
+    u = ((np.arange(R) + 0.5) / R).astype(np.float32)
+    k = np.array([(200, 1000, 1599)[r % 3] for r in range(R)])
+    # the weights are equal: of k tokens those before which less than top_p of the weight lies (the products
+    # below are not whole numbers), of m kept tokens the one at floor(u m)
+    for kw, m in ((dict(top_k=k), k), (dict(top_k=k, top_p=[0.6137] * R), np.ceil(np.float32(0.6137).astype(np.float64) * k))):
+        want = at + np.floor(u.astype(np.float64) * m).astype(np.int64)
+        for _ in range(10):
+            token, prob = run(x, u, **kw)
+            assert np.array_equal(token, want)
+            assert np.abs(prob * m - 1).max() <= 1e-6
