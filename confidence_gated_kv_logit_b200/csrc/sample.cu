@@ -59,6 +59,7 @@ constexpr int kAll = 2048;             // tokens down to a cut from which one CT
 constexpr int kGathers = 24;           // more than a row can need: two cuts, each at once, by parts of its bin and by six digits
 constexpr int kFew = 128;              // as many are ranked by comparing all with all
 static_assert(kAll <= kGather && kFew <= NT && kBins % NT == 0, "sizes of the first CTA's work");
+constexpr size_t kMaxShared = 220 * 1024;   // a wider part of a row stays in global memory
 constexpr int kMaxVocab = 1 << 20;     // index bits of the (logit, index) pair
 constexpr int kIndexBits = 20;
 
@@ -942,7 +943,7 @@ cudaError_t launch_cut(const SampleArgs& a0, int rows, cudaStream_t st) {
   a.chunk = ((a.vocab + CS - 1) / CS + 7) / 8 * 8;
   size_t smem = kSharedBytes<CS, CUT>;
   const size_t part = (size_t)a.chunk * 4;
-  a.staged = smem + part <= 220u * 1024 ? 1 : 0;
+  a.staged = smem + part <= kMaxShared ? 1 : 0;
   if (a.staged) smem += part;
   // Few rows spread over the SMs: where two CTAs an SM hold them all, as much
   // shared memory is asked for as keeps a third from joining them (33 rows of
@@ -952,7 +953,10 @@ cudaError_t launch_cut(const SampleArgs& a0, int rows, cudaStream_t st) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (10ll * rows * CS <= 18ll * sms) smem = std::max<size_t>(smem, 78 * 1024);
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<X, CS, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The limit is the kernel's, for every thread that calls it: always the same one, so that no call lowers it
+  // between another's setting and launch.
+  cudaError_t e =
+      cudaFuncSetAttribute(sample_kernel<X, CS, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxShared);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1023,6 +1027,7 @@ confkv_status confkv_sample(int32_t type, const void* logits, int64_t row_stride
     case CONFKV_F16: e = launch_sample<__half>(a, rows, st); break;
     default: e = launch_sample<__nv_bfloat16>(a, rows, st); break;
   }
+  if (e != cudaSuccess) (void)cudaGetLastError();   // not left for a later call
   return e == cudaSuccess ? CONFKV_OK : CONFKV_ERR_CUDA;
 }
 

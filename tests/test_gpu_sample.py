@@ -1,11 +1,14 @@
 """Sampling against the fp64 oracle on a B200."""
+import ctypes
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
-from confidence_gated_kv_logit_b200 import build, sample
+from confidence_gated_kv_logit_b200 import build, load_library, sample
 from oracle import sampling as oracle
 
 pytestmark = pytest.mark.gpu
@@ -272,3 +275,31 @@ def test_digits_with_more_ties_than_a_list_holds():
             token, prob = run(x, u, **kw)
             assert np.array_equal(token, want)
             assert np.abs(prob * m - 1).max() <= 1e-6
+
+
+class Job(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("u", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("token", ctypes.c_void_p), ("stream", ctypes.c_void_p),
+                ("calls", ctypes.c_int32), ("failed", ctypes.c_int32), ("sample", ctypes.c_void_p)]
+
+
+def test_threads_with_rows_of_different_sizes(tmp_path):
+    """Calls of one kernel from several threads, whose rows take different amounts of shared memory."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    helper = tmp_path / "sample_threads.so"
+    subprocess.run(["gcc", "-std=c99", "-O2", "-Wall", "-Werror", "-shared", "-fPIC", "-pthread", "-I",
+                    os.path.join(here, "..", "include"), os.path.join(here, "sample_threads.c"), "-o", str(helper)], check=True)
+    fn = ctypes.cast(load_library().confkv_sample, ctypes.c_void_p).value
+    work, jobs = [], (Job * 4)()
+    for i, (R, V) in enumerate([(2, 128256), (2, 50257), (40, 60001), (1, 9000)]):
+        x, u, top_p = logits_of(R, V, 40 + i).contiguous(), torch.rand(R, device="cuda"), torch.full((R,), 0.8, device="cuda")
+        want, got, stream = torch.empty(R, dtype=torch.int32, device="cuda"), torch.zeros(R, device="cuda").int(), torch.cuda.Stream()
+        sample(x, u, want, top_p=top_p)
+        work.append((x, u, top_p, want, got, stream))
+        jobs[i] = Job(x.data_ptr(), R, V, u.data_ptr(), top_p.data_ptr(), got.data_ptr(), stream.cuda_stream, 3000, 0, fn)
+    torch.cuda.synchronize()
+    assert ctypes.CDLL(str(helper)).run_threads(jobs, 4) == 0
+    torch.cuda.synchronize()
+    assert [j.failed for j in jobs] == [0] * 4
+    for _, _, _, want, got, _ in work:
+        assert torch.equal(want, got)
