@@ -25,11 +25,15 @@
 //      then by the bits of the (logit, index) pair), which gives the cut as such a
 //      pair; the weights of every warp's stretch of the row are summed, and the
 //      stretch that holds u times the total is scanned.
-// Weights are summed as integers (2^-30 of the largest for the cuts, 2^-40 for the
-// draw among gathered tokens) where the order of the additions is not fixed, in
+// Weights are summed as integers where the order of the additions is not fixed, in
 // fp64 and in a fixed order for the draw over a whole row, so two runs agree bit
-// for bit. The exponent (x - max) / (T ln 2) carries a correction for its rounding,
-// which alone would move the weights of far tokens by 1e-6.
+// for bit. The integers of the top-p cut are units of 2^-30 of a power of two near
+// the bin's own weights (of the largest weight of the row, a tail of 100000 light
+// tokens came out wrong by as much as it weighs); a bin's sum then goes into units of
+// 2^-42 of the largest, and what is left of the cut inside the bin back into the bin's.
+// Sums over a gathered list are units of 2^-40 of the largest. The exponent
+// (x - max) / (T ln 2) carries a correction for its rounding, which alone would move
+// the weights of far tokens by 1e-6.
 // Measured: 16 rows of 128256 fp32 with top-k 1000, top-p and min-p 31 us, 256 rows
 // with top-p 0.9 200 us (0.66 TB/s: the dozen barriers between a row's phases bound
 // it, with 37% of the issue slots used), 33 bf16 rows of 152064 with min-p
@@ -99,6 +103,7 @@ struct Shared {
   u64 cut_before, cut_here;
   int cut_bin, n_keep;
   int n_list;
+  uint32_t light;                       // of this CTA's tokens that a histogram passes over (2^-42)
   u64 list[kFew];
   uint32_t sel[2][kBins];               // select: the low and high 20 bits of the weights
   union {
@@ -116,7 +121,7 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 // Weights of one row: 2^((x - m) c), c = 1 / (T ln 2) as two floats.
 struct Weigher {
   float m, chi, clo;
-  float per;   // bins a factor of two, times -1 (a power of two)
+  float per;   // bins a factor of two, times -1 (a power of two, at least 32 where weights are summed by bin)
   // the exponent, rounded: descending in x, 0 at the maximum
   __device__ __forceinline__ float lead(float x) const { return __fmul_rn(__fsub_rn(x, m), chi); }
   __device__ __forceinline__ int bin(float d) const { return (int)fminf(__fmul_rn(d, per), (float)(kBins - 1)); }
@@ -133,12 +138,22 @@ struct Weigher {
     return d > -100.0f ? w : 0.0f;
   }
   __device__ __forceinline__ float weight(float x) const { return weight(x, lead(x)); }
+  // the weights of bin b lie between 2^-(e + 1) and 2^-e, e = fall(b) (the last bin's: anywhere below)
+  __device__ __forceinline__ int fall(int b) const { return b >> ((__float_as_int(-per) >> 23) - 127); }
 };
-// About how many tokens of bin b have `mass` units together (they weigh the same to 2%).
+// About how many tokens of bin b have `mass` (of 2^-42) together (they weigh the same to 2%, the last bin's aside).
 __device__ __forceinline__ float about(const Weigher& wt, u64 mass, int b) {
-  return (float)mass * ex2(((float)b + 0.5f) / -wt.per - 30.0f);
+  return (float)mass * ex2(((float)b + 0.5f) / -wt.per - 42.0f);
 }
-__device__ __forceinline__ uint32_t units(float w) { return min(__float2uint_rn(w * 0x1p30f), (1u << 30) - 1u); }
+// A weight in units of 2^-(30 + fall), fall that of its bin (below 2^30 units).
+__device__ __forceinline__ uint32_t units(float w, int fall) {
+  return min(__float2uint_rn(w * __int_as_float((127 + 30 + fall) << 23)), (1u << 30) - 1u);
+}
+// A bin's sum in units of 2^-42; and of a part of that, rounded up, in the bin's (not above its sum).
+__device__ __forceinline__ u64 to_common(u64 sum, int fall) { return (sum << 12) >> fall; }
+__device__ __forceinline__ u64 to_bin(u64 part, int fall) { return ((part << fall) + 0xfffull) >> 12; }
+// A weight in units of 2^-40, for sums over a list.
+__device__ __forceinline__ u64 fine_units(float w) { return min(__float2ull_rn(w * 0x1p40f), (1ull << 40) - 1ull); }
 
 // (logit, index) as an integer that descends along the order of the tokens.
 __device__ __forceinline__ u64 pair_key(float x, int i) {
@@ -252,12 +267,17 @@ __device__ __forceinline__ void collect(cg::cluster_group& cl, Shared<CS>& sh, T
 
 // Histogram of the tokens that `in` selects, by `digit`, summed over the
 // cluster: every CTA ends with its share of the bins and that share's sum.
-// Returns the sum of all. rest (counts): tokens of this thread in the last bin
-// that each4 passes over.
-template <bool MASS, int CS, class X, class In, class Digit>
+// Returns the sum of all. KIND: token counts; weights by bin (the digit is the
+// bin, the sums in units of 2^-42); weights of one bin's tokens by another digit
+// (the sums in that bin's units). rest: count, or weight in 2^-42, of this thread's
+// tokens in the last bin that each4 passes over.
+enum Kind { COUNT, BINS, WITHIN };
+template <Kind KIND, int CS, class X, class In, class Digit>
 __device__ __forceinline__ u64 histogram(cg::cluster_group& cl, Shared<CS>& sh, const Row<X>& row, const Weigher& wt,
-                                         In in, Digit digit, uint32_t rest = 0) {
+                                         In in, Digit digit, uint32_t rest = 0, int fall = 0) {
+  constexpr bool MASS = KIND != COUNT;
   for (int i = threadIdx.x; i < (MASS ? 2 : 1) * kBins; i += NT) (&sh.hist[0][0])[i] = 0;
+  if (KIND == BINS && threadIdx.x == 0) sh.light = 0;
   __syncthreads();
   each4(row, [&](const float (&x)[4], const int (&at)[4]) {
     int b[4];
@@ -267,11 +287,11 @@ __device__ __forceinline__ u64 histogram(cg::cluster_group& cl, Shared<CS>& sh, 
       const float d = wt.lead(x[k]);
       const bool mine = x[k] > -CUDART_INF_F && in(x[k], at[k], d);
       b[k] = digit(x[k], at[k], d);
-      w[k] = !mine ? 0u : MASS ? units(wt.weight(x[k], d)) : 1u;
+      w[k] = !mine ? 0u : MASS ? units(wt.weight(x[k], d), KIND == BINS ? wt.fall(b[k]) : fall) : 1u;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (MASS) {
+      if (MASS) {   // (at most 2^17 tokens a CTA)
         if (w[k] & 0x7fffu) atomicAdd(&sh.hist[0][b[k]], w[k] & 0x7fffu);
         if (w[k] >> 15) atomicAdd(&sh.hist[1][b[k]], w[k] >> 15);
       } else if (b[k] == kBins - 1) {   // the far tokens, most of a confident row: one address
@@ -281,22 +301,25 @@ __device__ __forceinline__ u64 histogram(cg::cluster_group& cl, Shared<CS>& sh, 
       }
     }
   });
-  if (!MASS) {
+  if (KIND != WITHIN) {
     rest = __reduce_add_sync(0xffffffffu, rest);
-    if (rest && (threadIdx.x & 31) == 0) atomicAdd(&sh.hist[0][kBins - 1], rest);
+    if (rest && (threadIdx.x & 31) == 0) atomicAdd(KIND == BINS ? &sh.light : &sh.hist[0][kBins - 1], rest);
   }
   cl.sync();
   constexpr int share = kBins / CS;
   const int rank = (int)cl.block_rank();
   u64 sum = 0;
   for (int i = threadIdx.x; i < share; i += NT) {
-    u64 v = 0;
+    const int bin = rank * share + i;
+    u64 v = 0, light = 0;
 #pragma unroll
     for (int r = 0; r < CS; ++r) {
       const Shared<CS>* o = cl.map_shared_rank(&sh, r);
-      v += o->hist[0][rank * share + i];
-      if (MASS) v += (u64)o->hist[1][rank * share + i] << 15;
+      v += o->hist[0][bin];
+      if (MASS) v += (u64)o->hist[1][bin] << 15;
+      if (KIND == BINS && bin == kBins - 1) light += o->light;
     }
+    if (KIND == BINS) v = to_common(v, wt.fall(bin)) + light;
     sh.slice[i] = v;
     sum += v;
   }
@@ -493,8 +516,8 @@ __device__ __forceinline__ u64 select(Shared<CS>& sh, int n, u64 target, int bit
   }
 }
 
-// The key at which the running count (or weight) reaches `target` (what is left
-// of it ahead of bin `bin`), by gathering the bin, split while it is too full:
+// The key at which the running count (or weight, in the bin's units) reaches
+// `target` (what is left of it ahead of bin `bin`), by gathering the bin, split while it is too full:
 // first into parts of its width, then by the keys' bits. here: the bin's count
 // or an estimate of it.
 template <bool MASS, int CS, class X, class In>
@@ -502,6 +525,8 @@ __device__ __noinline__ u64 exact_cut(cg::cluster_group& cl, Shared<CS>& sh, con
                                       const Weigher& wt, int* turn, int bin, u64 target, u64 here, In in) {
   int shift = kIndexBits + 32, sub = -1;
   u64 prefix = 0, before;
+  const int fall = MASS ? wt.fall(bin) : 0;
+  constexpr Kind KIND = MASS ? WITHIN : COUNT;
   auto mine = [&](float x, int i, float d) {
     return wt.bin(d) == bin && (sub < 0 || wt.sub_bin(d, bin) == sub) && in(x, i, d) &&
            (shift == kIndexBits + 32 || (pair_key(x, i0 + i) >> shift) == prefix);
@@ -509,13 +534,13 @@ __device__ __noinline__ u64 exact_cut(cg::cluster_group& cl, Shared<CS>& sh, con
   uint32_t found = here > kGather ? kGather + 1 : 0;
   while ((found > kGather || (found = gather(cl, sh, row, i0, wt, turn, mine)) > kGather) && shift > 0) {
     if (sub < 0) {
-      (void)histogram<MASS>(cl, sh, row, wt, mine, [&](float, int, float d) { return wt.sub_bin(d, bin); });
+      (void)histogram<KIND>(cl, sh, row, wt, mine, [&](float, int, float d) { return wt.sub_bin(d, bin); }, 0, fall);
       sub = find_bin(cl, sh, target, &before, &here);
     } else {
       const int bits = min(10, shift), next = shift - bits, top = (1 << bits) - 1;
-      (void)histogram<MASS>(cl, sh, row, wt, mine, [&](float x, int i, float) {
+      (void)histogram<KIND>(cl, sh, row, wt, mine, [&](float x, int i, float) {
         return top - (int)((pair_key(x, i0 + i) >> next) & (unsigned)top);
-      });
+      }, 0, fall);
       const int b = find_bin(cl, sh, target, &before, &here);
       prefix = (prefix << bits) | (unsigned)(top - b);
       shift = next;
@@ -526,7 +551,7 @@ __device__ __noinline__ u64 exact_cut(cg::cluster_group& cl, Shared<CS>& sh, con
   if (cl.block_rank() == 0) {
     const u64 k = select(sh, min((int)found, kGather), target, kIndexBits + 32,
                          [&](u64 k) { return wt.sub_bin(wt.lead(key_logit(k)), bin); },
-                         [&](u64 k) { return MASS ? (u64)units(wt.weight(key_logit(k))) : 1ull; }, [](u64 k) { return k; });
+                         [&](u64 k) { return MASS ? (u64)units(wt.weight(key_logit(k)), fall) : 1ull; }, [](u64 k) { return k; });
     if (threadIdx.x == 0) sh.key = k;
   }
   cl.sync();
@@ -534,29 +559,34 @@ __device__ __noinline__ u64 exact_cut(cg::cluster_group& cl, Shared<CS>& sh, con
 }
 
 // The first CTA finishes a row from the tokens in `cand`, which are the first n
-// of the order: top-k, top-p (mass: the weight of K1, or 0: that of the list's
-// first top_k), min-p and the draw.
+// of the order: top-k, top-p, min-p and the draw. cut_bin: where the cut of top-p
+// falls, cut_target in that bin's units; -1: at top_p of the weight of the list's
+// first top_k.
 template <int CS>
-__device__ __noinline__ void finish(Shared<CS>& sh, int n, const Weigher& wt, int top_k, float top_p, u64 mass,
-                                    float least, float u, int vocab, int32_t* token, float* prob) {
+__device__ __noinline__ void finish(Shared<CS>& sh, int n, const Weigher& wt, int top_k, float top_p, int cut_bin,
+                                    u64 cut_target, float least, float u, int vocab, int32_t* token, float* prob) {
   if (n > kFew) {
     auto bin = [&](u64 k) { return wt.bin(wt.lead(key_logit(k))); };
     auto same = [](u64 k) { return k; };
     u64 low = 0, sum = 0, all;   // keys from `low` on are kept
     if (top_k > 0 && top_k < n) low = select(sh, n, (u64)top_k, kIndexBits + 32, bin, [](u64) { return 1ull; }, same);
     if (top_p < 1.0f) {
-      auto weight = [&](u64 k) { return k >= low ? (u64)units(wt.weight(key_logit(k))) : 0ull; };
-      if (mass == 0) {
+      if (cut_bin < 0) {
+        auto weight = [&](u64 k) { return k >= low ? fine_units(wt.weight(key_logit(k))) : 0ull; };
         for (int i = threadIdx.x; i < n; i += NT) sum += weight(sh.cand[i]);
-        (void)block_prefix(sh.scan, sum, &mass);
+        (void)block_prefix(sh.scan, sum, &all);
+        const u64 target = max(1ull, min(all, (u64)ceil((double)top_p * (double)all)));
+        low = max(low, select(sh, n, target, kIndexBits + 32, bin, weight, same));
+      } else {   // (every token of the bins before it is above that key)
+        const int fall = wt.fall(cut_bin);
+        low = select(sh, n, cut_target, kIndexBits + 32, [&](u64 k) { return wt.sub_bin(wt.lead(key_logit(k)), cut_bin); },
+                     [&](u64 k) { return bin(k) == cut_bin ? (u64)units(wt.weight(key_logit(k)), fall) : 0ull; }, same);
       }
-      const u64 target = max(1ull, min(mass, (u64)ceil((double)top_p * (double)mass)));
-      low = max(low, select(sh, n, target, kIndexBits + 32, bin, weight, same));
     }
-    // the draw in units of 2^-40 of the largest weight, exact whatever the order of the additions
+    // the draw in the same units, exact whatever the order of the additions
     auto weight = [&](u64 k) {
       const float x = key_logit(k);
-      return k >= low && x >= least ? min(__float2ull_rn(wt.weight(x) * 0x1p40f), (1ull << 40) - 1ull) : 0ull;
+      return k >= low && x >= least ? fine_units(wt.weight(x)) : 0ull;
     };
     sum = 0;
     for (int i = threadIdx.x; i < n; i += NT) sum += weight(sh.cand[i]);
@@ -575,24 +605,26 @@ __device__ __noinline__ void finish(Shared<CS>& sh, int n, const Weigher& wt, in
   if (top_k > 0) n = min(n, top_k);
   constexpr int per = (kFew + NT - 1) / NT;
   const int j0 = threadIdx.x * per;
-  u64 key[per];
+  u64 key[per], mass[per];
   float w[per];
   u64 sum = 0, all;
   if (threadIdx.x == 0) sh.n_keep = n;
+  const int fall = cut_bin < 0 ? 0 : wt.fall(cut_bin);
 #pragma unroll
   for (int k = 0; k < per; ++k) {
     key[k] = j0 + k < n ? sh.cand[j0 + k] : 0;
-    w[k] = j0 + k < n ? wt.weight(key_logit(key[k])) : 0.0f;
-    sum += units(w[k]);
+    const float x = key_logit(key[k]);
+    w[k] = j0 + k < n ? wt.weight(x) : 0.0f;
+    mass[k] = cut_bin < 0 ? fine_units(w[k]) : wt.bin(wt.lead(x)) == cut_bin ? units(w[k], fall) : 0;
+    sum += mass[k];
   }
   u64 run = block_prefix(sh.scan, sum, &all);
-  if (mass == 0) mass = all;
-  const u64 target = top_p < 1.0f ? max(1ull, min(mass, (u64)ceil((double)top_p * (double)mass))) : ~0ull;
+  if (cut_bin < 0) cut_target = max(1ull, min(all, (u64)ceil((double)top_p * (double)all)));
 #pragma unroll
   for (int k = 0; k < per; ++k) {
-    const bool in = j0 + k < n && run < target && key_logit(key[k]) >= least;
+    const bool in = j0 + k < n && (top_p >= 1.0f || run < cut_target) && key_logit(key[k]) >= least;
     if (j0 + k < n && !in) atomicMin(&sh.n_keep, j0 + k);
-    run += units(w[k]);
+    run += mass[k];
   }
   __syncthreads();
   n = sh.n_keep;   // at least the first token
@@ -773,76 +805,89 @@ __global__ void __launch_bounds__(NT, CUT ? 2 : 3) sample_kernel(const SampleArg
 
   // ---- the cuts of top-k and top-p ----
   // Where most tokens of a row weigh less than 2^-31 of the largest, as in a
-  // confident model's, the passes below go over the others alone (256 rows of
-  // 128256, top-p 0.9: 237 us without the list, 217 with it; not for fewer than
-  // five fours a thread, where making it costs as much as it saves).
-  uint32_t rest = 0;
+  // confident model's, the passes below go over the others alone, as long as no cut
+  // falls past those (256 rows of 128256, top-p 0.9: 283 us without the list, 214 with
+  // it; not for fewer than five fours a thread, where making it costs as much as it saves).
+  uint32_t rest = 0, light = 0;   // tokens of this thread that are passed over: their count and weight (2^-42)
   const bool cuts = CUT && ((top_k > 0 && top_k < a.vocab) || top_p < 1.0f);
   const int fours = (row.n + 4 * NT - 1) / (4 * NT);
   if (cuts && wt.per == -32.0f && row.s && fours > 4 && fours <= 16) {
     int finite = 0, seen = 0;
+    float sum = 0.0f;
     each4(row, [&](const float (&x)[4], const int (&)[4]) {
       uint32_t m = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        const float d = wt.lead(x[k]);
+        const bool far = !(d * wt.per < (float)(kBins - 1));
         finite += x[k] > -CUDART_INF_F;
-        m |= (uint32_t)(wt.lead(x[k]) * wt.per < (float)(kBins - 1)) << k;
+        m |= (uint32_t)!far << k;
+        sum += far ? ex2(d) : 0.0f;
       }
       row.near |= (u64)m << seen;
       seen += 4;
     });
     const int mine = __popcll(row.near);
     row.few = 3 * ((__reduce_max_sync(0xffffffffu, mine) + 3) / 4) <= 2 * fours;
-    rest = row.few ? (uint32_t)(finite - mine) : 0;
+    if (row.few) {
+      rest = (uint32_t)(finite - mine);
+      light = __float2uint_rn(sum * 0x1p42f);
+    }
   }
   Cut cut{-CUDART_INF_F, kMaxVocab};
   bool done = false;
   int turn = 0;
   if (top_k > 0 && top_k < a.vocab) {
     auto any = [](float, int, float) { return true; };
-    const u64 count = histogram<false>(cl, sh, row, wt, any, [&](float, int, float d) { return wt.bin(d); }, rest);
+    const u64 count = histogram<COUNT>(cl, sh, row, wt, any, [&](float, int, float d) { return wt.bin(d); }, rest);
     if ((u64)top_k < count) {
       u64 before, here;
       int b = find_bin(cl, sh, (u64)top_k, &before, &here);
-      const bool few = row.few;
       const float per = wt.per;
+      light = 0;   // past the cut, or (below) no longer passed over
       if (b == kBins - 1 && per == -32.0f) {
         // the cut lies past the bins (a confident row): all tokens again, in wider
         // ones that reach down to the smallest, or for 512 factors of two
         row.few = false;
         while (wt.per < -2.0f && wt.lead(mn) * wt.per >= (float)(kBins - 1)) wt.per *= 0.5f;
-        (void)histogram<false>(cl, sh, row, wt, any, [&](float, int, float d) { return wt.bin(d); });
+        (void)histogram<COUNT>(cl, sh, row, wt, any, [&](float, int, float d) { return wt.bin(d); });
         b = find_bin(cl, sh, (u64)top_k, &before, &here);
       }
       if (before + here <= kAll) {
         const uint32_t n = gather(cl, sh, row, i0, wt, &turn, [&](float, int, float d) { return wt.bin(d) <= b; });
-        if (rank == 0) finish(sh, (int)n, wt, top_k, top_p, 0, least, u, a.vocab, a.token + r, a.prob ? a.prob + r : nullptr);
+        if (rank == 0) finish(sh, (int)n, wt, top_k, top_p, -1, 0, least, u, a.vocab, a.token + r, a.prob ? a.prob + r : nullptr);
         done = true;
       } else {
         const u64 k = exact_cut<false>(cl, sh, row, i0, wt, &turn, b, (u64)top_k - before, here, any);
         cut = Cut{key_logit(k), key_index(k)};
       }
-      row.few = few;
       wt.per = per;
     }
   }
   if (!done && top_p < 1.0f) {
     auto in_k = [&](float x, int i, float) { return cut.keeps(x, i0 + i); };
-    const u64 mass = histogram<true>(cl, sh, row, wt, in_k, [&](float, int, float d) { return wt.bin(d); });
-    const u64 target = max(1ull, min(mass, (u64)ceil((double)top_p * (double)mass)));
+    auto by_bin = [&](float, int, float d) { return wt.bin(d); };
+    auto cut_of = [&](u64 mass) { return max(1ull, min(mass, (u64)ceil((double)top_p * (double)mass))); };
+    u64 target = cut_of(histogram<BINS>(cl, sh, row, wt, in_k, by_bin, light));
     u64 before, here;
-    const int b = find_bin(cl, sh, target, &before, &here);
+    int b = find_bin(cl, sh, target, &before, &here);
+    if (b == kBins - 1 && wt.per == -32.0f) {   // among the tokens passed over, if there are any: all of them again
+      row.few = false;
+      target = cut_of(histogram<BINS>(cl, sh, row, wt, in_k, by_bin));
+      b = find_bin(cl, sh, target, &before, &here);
+    }
+    target = to_bin(target - before, wt.fall(b));
     // the tokens down to the bin are at most as many as weigh what the bin's do; a bin
     // that is itself too full is not gathered to find that out
     const float in_bin = about(wt, here, b);
     uint32_t n = kAll + 1;
-    if (in_bin < (float)kAll && (float)before * 0x1p-30f < (float)kAll)
+    if (in_bin < (float)kAll && (float)before * 0x1p-42f < (float)kAll)
       n = gather(cl, sh, row, i0, wt, &turn, [&](float x, int i, float d) { return wt.bin(d) <= b && cut.keeps(x, i0 + i); });
     if (n <= kAll) {
-      if (rank == 0) finish(sh, (int)n, wt, 0, top_p, mass, least, u, a.vocab, a.token + r, a.prob ? a.prob + r : nullptr);
+      if (rank == 0) finish(sh, (int)n, wt, 0, top_p, b, target, least, u, a.vocab, a.token + r, a.prob ? a.prob + r : nullptr);
       done = true;
     } else {
-      const u64 k = exact_cut<true>(cl, sh, row, i0, wt, &turn, b, target - before, (u64)in_bin, in_k);
+      const u64 k = exact_cut<true>(cl, sh, row, i0, wt, &turn, b, target, (u64)in_bin, in_k);
       cut = Cut{key_logit(k), key_index(k)};
     }
   }

@@ -463,9 +463,11 @@ CONFKV_API confkv_status confkv_rope(const confkv_rope_table* table, int32_t bat
  *   token_out  int32 [rows];  prob_out  fp32 [rows], optional
  * A row with a NaN or +inf logit, without a logit above -inf, or with a NaN
  * parameter, a negative or infinite temperature, or u outside [0, 1), gets
- * token -1 and probability 0. Weights are fp32 (about 2^-22 relative); their sums
- * are fp64, or integers of 2^-30 (the top_p cut) or 2^-40 (the draw) of the largest, and do not
- * depend on timing: a call repeated gives the same bits.
+ * token -1 and probability 0. Weights are fp32: off by about 2^-22 of their value, and by
+ * 2^-24 |x_i - max x| / T of it where that difference of two fp32 logits is not exact. Their sums
+ * are fp64 over fours added in fp32, or integers: for the top_p cut of 2^-30 of each weight's own
+ * magnitude and 2^-32 of the largest weight over the whole row, over up to 2048 gathered tokens
+ * of 2^-40 of the largest. None depends on timing: a call repeated gives the same bits.
  * CAPACITY: vocab above 1048576. rows of 0 does nothing. */
 CONFKV_API confkv_status confkv_sample(int32_t type, const void* logits, int64_t row_stride, int32_t rows,
                                        int32_t vocab, const float* u, const float* temperature, const int32_t* top_k,

@@ -303,3 +303,30 @@ def test_threads_with_rows_of_different_sizes(tmp_path):
     assert [j.failed for j in jobs] == [0] * 4
     for _, _, _, want, got, _ in work:
         assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("V", [2000, 50257, 128256, 400001])
+@pytest.mark.parametrize("tail", [-19.0, -21.4, -21.6, -24.5])
+@pytest.mark.parametrize("p", [0.5, 0.9999, 0.99995, 0.99998, 0.9999995])
+def test_long_light_tails(V, tail, p):
+    """One token over a tail that weighs 6e-9 to 2e-11 of it a token: top_p cuts by the tail's sum."""
+    x = torch.full((1, V), tail, device="cuda")
+    x[0, 0] = 0.0
+    u, w1 = np.nextafter(np.float32(1), np.float32(0)), math.exp(tail)
+    idx, w = oracle.kept_set(x[0].cpu().numpy(), top_p=np.float32(p))
+    (token,), (prob,) = run(x, [0.0], top_p=[p])
+    (far,), _ = run(x, [u], top_p=[p])
+    # What may move the border, as a share of the largest weight: half a unit of 2^-40 a token of the row, in the
+    # cut and again in the draw; 2^-22 of the tail's sum, for fp32 weights. Then, in tokens: four weights that are
+    # added in fp32 before fp64 takes them, where the largest swallows the other three; one for a border's two sides.
+    off = 2 * V * 2.0 ** -41 + V * w1 * 2.0 ** -22
+    if len(idx) == 1:
+        # (no border near: what is missing to the first token's weight is more than that)
+        assert 1 - float(np.float32(p)) * (1 + (V - 1) * w1) > off + 2.0 ** -23
+        assert far == 0 and prob == 1
+        return
+    # the last kept token but those that weigh 1 - u of the total together
+    want = len(idx) - 1 - int((1 - float(u)) * w.sum() / w1)
+    assert abs(far - max(want, 0)) <= off / w1 + 5
+    # the largest token's share is one over the sum of the kept weights (and an fp32 number below 1)
+    assert token == 0 and abs(1 / float(prob) - w.sum()) <= off + 5 * w1 + 2.0 ** -24
