@@ -248,7 +248,8 @@ confkv_status confkv_create(int32_t layers, int32_t kv_heads, int32_t q_heads, i
     h->max_eff[l] = eff;
     need = std::max<long long>(need, eff);
   }
-  if (p.mode == CONFKV_MODE_FIXED) need = p.fixed_budget;
+  // a fixed budget holds that many tokens of any prompt, and takes a draft's on top
+  if (p.mode == CONFKV_MODE_FIXED) need = (long long)p.fixed_budget + CONFKV_MAX_NODES;
   const long long cap_ll = round_up(need + 2, 64);
   if (cap_ll > (1ll << 28)) {
     delete h;

@@ -264,7 +264,8 @@ CONFKV_API confkv_status confkv_tree_attn(confkv_handle* h, int32_t layer, int32
  *          (NULL: tokens)
  * A count or row out of range sets the device word (ERR_DEVICE) and that
  * sequence gets none of its tokens. CAPACITY if `tokens` more could overflow
- * the cache (size max_prefill for the longest draft beyond the budget). */
+ * the cache: in confidence mode size max_prefill for the longest draft beyond
+ * the budget; a fixed-budget cache has room for CONFKV_MAX_NODES beyond its own. */
 CONFKV_API confkv_status confkv_append(confkv_handle* h, int32_t layer, int32_t tokens, int32_t rows, const void* k,
                                        const void* v, const float* prio, const int32_t* index, const int32_t* counts,
                                        void* stream);

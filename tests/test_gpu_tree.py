@@ -583,3 +583,32 @@ def test_refusals():
     refused(1, hf.tree_attn, q[:1], kd[:1], vd[:1], mask[:1], out[:1], layer=0, track=True)
     refused(1, hf.append, kd[:1], vd[:1], layer=0)
     hf.close()
+
+
+@pytest.mark.parametrize("budget", [62, 100, 126, 1022])
+@pytest.mark.parametrize("int8", [0, 1])
+def test_fixed_budgets_have_room_for_the_widest_draft(budget, int8):
+    """Fixed mode: a cache at its budget takes CONFKV_MAX_NODES tokens, and eviction brings it back."""
+    p = Params(mode="fixed", fixed_budget=budget, protect_last=20, n_sink=3, fp16_window=16, int8=bool(int8))
+    g = synth.generator(40, "cuda")
+    Hkv, D, T, N = 2, 64, budget + 30, 64
+    h = ConfKV(1, Hkv, 2, D, **c_params(p, 2, T))
+    k, v = synth.prefill_kv(2, Hkv, T, D, g, "cuda")
+    pr = synth.priorities((2, Hkv, T), g, "cuda")
+    h.prefill(k, v, [T, T], layer=0, priority=pr)
+    segs = {(b, kv): prefill_segment(k[b, kv].cpu().numpy(), v[b, kv].cpu().numpy(), pr[b, kv].cpu().numpy(), p, (0, b, kv))
+            for b in range(2) for kv in range(Hkv)}
+    for counts in ([N, N], [1, 33]):
+        _, kd, vd = drafts((2,), N, 2, Hkv, D, g)
+        pn = synth.priorities((2, N, Hkv), g, "cuda")
+        h.append(kd, vd, layer=0, prio=pn, counts=torch.tensor(counts, dtype=torch.int32, device="cuda"))
+        h.evict_compact()
+        for (b, kv), seg in segs.items():
+            n = counts[b]
+            append_rows(seg, kd[b, :n, kv].cpu().numpy(), vd[b, :n, kv].cpu().numpy(), pn[b, :n, kv].cpu().numpy(), p)
+            segs[b, kv] = seg = evict_compact_segment(seg, budget, p)
+            got = logical_segment(h.export_segment(0, b, kv))
+            for key in ("pos", "is_fp16", "k8", "v8", "ks", "vs", "k16", "v16", "score_src", "next_pos"):
+                assert np.array_equal(got[key], getattr(seg, key)), (counts, b, kv, key)
+    assert h.last_error() == 0
+    h.close()
