@@ -59,7 +59,8 @@ struct TileAux {
 };
 
 struct Bars {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], aux_full[kAux], aux_empty[kAux], s_full[2], p_full[2], o_done[2];
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], aux_full[kAux], aux_empty[kAux], s_full[2], p_full[2], o_done[2],
+      drained;
 };
 
 template <int D>
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const Cache c, co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 256);
+    mbar_init(&bar.drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4);
       mbar_init(&bar.k_empty[i], 1);
@@ -419,9 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const Cache c, co
       // on an abort too, nothing of this lane's may be in flight when the CTA ends
       if (!ok) {
         *abort_flag = 1;
-        tc_commit(&bar.q_full, leader);
-        for (int k = 0; k < 4096 && !mbar_try_wait(&bar.q_full, 1); ++k) {
-        }
+        tc_commit(&bar.drained, leader);
+        (void)mbar_wait_bounded(&bar.drained, 0);
       }
     }
     // ------------------------------ scales ------------------------------
