@@ -612,3 +612,146 @@ def test_fixed_budgets_have_room_for_the_widest_draft(budget, int8):
                 assert np.array_equal(got[key], getattr(seg, key)), (counts, b, kv, key)
     assert h.last_error() == 0
     h.close()
+
+
+@pytest.mark.parametrize("single", [0, 1])
+@pytest.mark.parametrize("Hq,N,lens", [(8, 8, [300, 41, 0]),          # 32 rows per KV head: the last of the small kernel
+                                       (8, 9, [300, 41, 0]),          # 36 rows: the first of the other
+                                       (8, 40, [300, 41, 700]),       # 160: each softmax group has rows of its own
+                                       (16, 64, [90, 500, 1]),        # 512: two row tiles
+                                       (2, 64, [9000, 20, 4100])])    # 64, over many splits
+def test_tracked_roots_of_wide_trees(single, Hq, N, lens):
+    """The root's mass on both sides of the kernels' border, for counts from 0 to all, against decode attention."""
+    Hkv, D, B = 2, 128, 3
+    for counts in ([N, 1, max(2, N - 3)], [0, N, 1]):
+        ha, hb = (build_handle(Hkv, Hq, D, lens, synth.generator(41, "cuda"), decode=5, single_stream=single) for _ in range(2))
+        g = synth.generator(42, "cuda")
+        before = [logical_segment(hb.export_segment(0, 0, kv))["score_src"] for kv in range(Hkv)]
+        q, kd, vd = drafts((1, B), N, Hq, Hkv, D, g)
+        masks = tree_masks(B, N, np.random.RandomState(4))
+        out, lse = torch.full_like(q, 7.0), torch.full((1, B, N, Hq), 7.0, device="cuda")
+        rows = [[cached(hb, 0, b, kv) for kv in range(Hkv)] for b in range(B)]
+        ct = torch.tensor(counts, dtype=torch.int32, device="cuda")
+        hb.tree_attn(q, kd, vd, dev_mask(masks), out, counts=ct, lse_out=lse, track=True)
+        for b in range(B):
+            if counts[b] == 0:
+                continue
+            for kv in range(Hkv):
+                G, (k, v) = Hq // Hkv, rows[b][kv]
+                want, wl, spread, reach = attend_nodes(
+                    q[0, b, :1, kv * G:kv * G + G].cpu().numpy(), k, v, kd[0, b, :1, kv].cpu().numpy(),
+                    vd[0, b, :1, kv].cpu().numpy(), [1])
+                got = out[0, b, 0, kv * G:kv * G + G].double().cpu().numpy()
+                delta = 24 * 2.0 ** -23 * reach[0][:, None]       # as in check_segment
+                big = float(np.abs(v).max()) if len(v) else 0.0
+                tol = 2.0 ** -11 * np.abs(want[0]) + 2.0 ** -21 * spread[0] + 2 * delta * spread[0] + \
+                    len(v) * 2.0 ** -31 * max(big, 1.0) + 2.0 ** -25
+                assert (np.abs(got - want[0]) <= tol).all()
+        for b in range(B):
+            assert (out[0, b, counts[b]:] == 7.0).all() and (lse[0, b, counts[b]:] == 7.0).all()
+        ha.decode_attn(q[:, :, 0].contiguous(), kd[:, :, 0].contiguous(), vd[:, :, 0].contiguous(),
+                       torch.empty((1, B, Hq, D), device="cuda"))
+        hb.append(kd, vd, index=torch.zeros((B, 1), dtype=torch.int32, device="cuda"))
+        for b in range(B):
+            for kv in range(Hkv):
+                a, t = (logical_segment(h.export_segment(0, b, kv)) for h in (ha, hb))
+                assert np.array_equal(a["pos"], t["pos"])
+                if counts[b]:
+                    np.testing.assert_allclose(t["score_src"][:-1], a["score_src"][:-1], rtol=2 * RTOL_EMA, atol=ATOL_EMA)
+                else:          # no node, no mass
+                    np.testing.assert_array_equal(t["score_src"][:-1], (np.float32(0.9) * before[kv]).astype(np.float32))
+        assert ha.last_error() == 0 and hb.last_error() == 0
+        ha.close()
+        hb.close()
+
+
+@pytest.mark.parametrize("N,G,kw", [(8, 4, {}), (9, 4, {}), (33, 2, {}), (33, 8, {}), (64, 8, {}), (12, 8, dict(int8_enable=0)),
+                                    (40, 4, dict(int8_enable=0)), (4, 4, dict(int8_enable=0))])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_unseen_nodes_stay_out_of_every_kernel(N, G, kw, D):
+    """NaN and inf of a node's key and value, and of rows past the count, on both sides of the kernels' border and
+    in the second tile of rows; a count out of range beside it."""
+    g = synth.generator(43, "cuda")
+    h = build_handle(2, 2 * G, D, [300, 3, 40], g, **kw)
+    q, kd, vd = drafts((3,), N, 2 * G, 2, D, g)
+    masks = np.zeros((3, N), np.uint64)
+    for i in range(N):
+        masks[:, i] = 1 | 1 << i                                     # a root and its children
+    ct = torch.tensor([N, N - 2, N], dtype=torch.int32, device="cuda")
+    clean = torch.full_like(q, 7.0)
+    h.tree_attn(q, kd, vd, dev_mask(masks), clean, 0, counts=ct)
+    assert torch.isfinite(clean).all()
+    kd2, vd2 = kd.clone(), vd.clone()
+    vd2[0, 1] = math.inf
+    vd2[0, 2, :, 7] = math.nan
+    kd2[0, N - 1] = math.nan
+    vd2[0, 3, :, 5] = -math.inf
+    kd2[1, N - 2:] = math.nan                                        # past the count
+    vd2[1, N - 2:] = -math.inf
+    out, lse = torch.full_like(q, 7.0), torch.full((3, N, 2 * G), 7.0, device="cuda")
+    ct[2] = N + 1
+    h.tree_attn(q, kd2, vd2, dev_mask(masks), out, 0, counts=ct, lse_out=lse)
+    for i in range(N):
+        if i not in (1, 2, 3, N - 1):
+            assert torch.equal(out[0, i], clean[0, i]), i
+    assert torch.equal(out[1], clean[1])
+    assert (out[0, 1] == math.inf).all()
+    assert torch.isnan(out[0, 2, :, 7]).all() and torch.equal(out[0, 2, :, :7], clean[0, 2, :, :7])
+    if N > 4:                                                        # (else node 3 is the one whose key is NaN)
+        assert (out[0, 3, :, 5] == -math.inf).all() and torch.equal(out[0, 3, :, 6:], clean[0, 3, :, 6:])
+    assert torch.isnan(out[0, N - 1]).all() and torch.isnan(lse[0, N - 1]).all()
+    assert torch.isfinite(lse[0, :N - 1]).all()
+    assert (out[2] == 7.0).all() and (lse[2] == 7.0).all()
+    assert h.last_error_detail()[:2] == (7, 207) and h.last_error(clear=True) == 7
+    h.close()
+
+
+@pytest.mark.parametrize("kw", [dict(W=1), dict(W=200), dict(W=64), dict(int8_enable=0), dict(compact=1), dict(compact=2),
+                                dict(mode=1, fixed_budget=100, n_sink=4, protect_last=20, int8_enable=0),
+                                dict(mode=1, fixed_budget=200, protect_last=40)],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N", [3, 8, 80])
+def test_layouts_after_evictions_of_every_width(kw, D, N):
+    """Caches as decoding leaves them: few rows per KV head, as many as the small kernel takes, and both row tiles."""
+    g = synth.generator(44, "cuda")
+    lens, Hq = [260, 140, 5], 8
+    if N == 80:
+        N, Hq = 40, 16
+    h = build_handle(2, Hq, D, lens, g, decode=45, **kw)
+    r = run_tree(h, N, lens, g, counts=[N, N - 1, 1])
+    for b in range(3):
+        for kv in range(2):
+            check_segment(h, *r, 0, b, kv)
+    assert h.last_error() == 0
+    h.close()
+
+
+@pytest.mark.parametrize("single", [0, 1])
+@pytest.mark.parametrize("compact", [0, 1, 2])
+@pytest.mark.parametrize("N", [4, 20])
+def test_eviction_right_after_a_tracked_tree(single, compact, N):
+    """A draft of which nothing is accepted: the deferred pass goes into the eviction, or runs before it."""
+    kw = dict(single_stream=single, compact=compact, n_low=40, n_high=40, protect_last=8)
+    hs = [build_handle(2, 8, 64, [300, 45], synth.generator(45, "cuda"), **kw) for _ in range(2)]
+    for step in range(3):
+        g = synth.generator(46 + step, "cuda")
+        q, kd, vd = drafts((1, 2), N, 8, 2, 64, g)
+        mask = dev_mask(tree_masks(2, N, np.random.RandomState(step)))
+        for i, h in enumerate(hs):
+            h.tree_attn(q, kd, vd, mask, torch.empty_like(q), track=True)
+            if i:
+                h.query()                                            # applies the deferred pass on its own
+            if step:
+                h.append(kd, vd, index=torch.zeros((2, 1), dtype=torch.int32, device="cuda"),
+                         counts=torch.zeros(2, dtype=torch.int32, device="cuda"))
+            h.evict_compact()
+        for b in range(2):
+            for kv in range(2):
+                x, y = (logical_segment(h.export_segment(0, b, kv)) for h in hs)
+                for key in ("pos", "is_fp16", "k8", "v8", "ks", "vs", "k16", "v16", "score_src", "next_pos"):
+                    assert np.array_equal(x[key], y[key]), (step, b, kv, key)
+        assert len(x["pos"]) == 40
+    assert all(h.last_error() == 0 for h in hs)
+    for h in hs:
+        h.close()
