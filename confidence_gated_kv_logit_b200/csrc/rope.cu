@@ -376,6 +376,20 @@ cudaError_t launch_x(const RopeArgs& a, int y_type, bool half, bool vec, cudaStr
   }
 }
 
+// Whether the rows of an output (their strides in elements) lie apart: in the
+// order of the strides, each dimension steps over all that those before it span.
+bool rows_apart(int D, int batch, long long yb, int tokens, long long yt, int heads, long long yh) {
+  struct { int n; long long step; } d[3] = {{batch, yb}, {tokens, yt}, {heads, yh}};
+  std::sort(d, d + 3, [](const auto& a, const auto& b) { return a.step < b.step; });
+  __int128 span = D;
+  for (const auto& x : d) {
+    if (x.n <= 1) continue;
+    if (x.step < span) return false;
+    span += (__int128)(x.n - 1) * x.step;
+  }
+  return true;
+}
+
 bool finite_pos(double v) { return std::isfinite(v) && v > 0.0; }
 
 }  // namespace
@@ -482,9 +496,9 @@ confkv_status confkv_rope(const confkv_rope_table* table, int32_t batch, int32_t
     if (px % xs || py % ys || pw % 4) return CONFKV_ERR_ARG;
     if (r->x_batch < 0 || r->x_token < 0 || r->x_head < 0 || r->y_batch < 0 || r->y_token < 0 || r->y_head < 0)
       return CONFKV_ERR_ARG;
-    // distinct rows must be written to distinct places
-    if ((r->heads > 1 && r->y_head < D) || (tokens > 1 && r->y_token < D) || (batch > 1 && r->y_batch < D))
-      return CONFKV_ERR_ARG;
+    // distinct rows must be written to distinct places, those of q and k among them
+    if (!rows_apart(D, batch, r->y_batch, tokens, r->y_token, r->heads, r->y_head)) return CONFKV_ERR_ARG;
+    if (sd == 1 && r->y == in[0]->y) return CONFKV_ERR_ARG;
     if (px == py && (x_type != y_type || r->x_batch != r->y_batch || r->x_token != r->y_token || r->x_head != r->y_head))
       return CONFKV_ERR_ARG;
     const long long ex = 16 / (long long)xs, ey = 16 / (long long)ys;

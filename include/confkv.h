@@ -412,8 +412,10 @@ typedef struct {
 /* The rows of one side (queries, or keys): [batch][tokens][heads][head_dim]
  * with the last dimension contiguous and the other strides given in elements
  * (not negative; a column block of a packed projection, or a
- * [batch][heads][tokens][head_dim] buffer, are such rows). y may be x itself
- * with the same type and strides; any other overlap is not allowed. */
+ * [batch][heads][tokens][head_dim] buffer, are such rows). Rows of y lie apart:
+ * in the order of their strides, each dimension steps over all that the ones
+ * before it span (ARG otherwise). y may be x itself with the same type and
+ * strides; any other overlap, of the two sides' y among them, is not allowed. */
 typedef struct {
   const void* x;
   void* y;

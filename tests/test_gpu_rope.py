@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from confidence_gated_kv_logit_b200 import Rope, build
+from confidence_gated_kv_logit_b200 import ConfKVError, Rope, build
 from oracle.rope import frequencies
 
 pytestmark = pytest.mark.gpu
@@ -211,3 +211,27 @@ def test_odd_parts_of_many_heads(D, rd, layout):
     assert torch.equal(qkv[..., rd:], x[..., rd:])
     want, size = oracle(x[..., :rd], pos, {}, rd, layout, None, 0.0)
     check(qkv[..., :rd], want, size, torch.float16)
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    """Every row of an output has a place of its own, whichever way its strides go."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    B, T, H, D = 2, 4, 3, 64
+    q = make(B, T, H, D, torch.float16, g)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32).repeat(B, 1)
+    r = Rope(D)
+    room = torch.zeros(B * T * H * D * 4, dtype=torch.float16, device="cuda")
+    for strides in ((T * H * D, D, D), (T * D, H * D, D), (D, B * D, D), (T * H * D, H * D, D - 1), (8 * D, 2 * D, 3 * D)):
+        with pytest.raises(ConfKVError) as e:
+            r.apply(q, None, pos, room.as_strided(q.shape, strides + (1,)))
+        assert e.value.status == 1
+    with pytest.raises(ConfKVError) as e:      # one output for both sides
+        r.apply(q, q, pos, room.as_strided(q.shape, q.stride()), room.as_strided(q.shape, q.stride()))
+    assert e.value.status == 1
+    assert (room == 0).all()
+    # rows apart from one another, in every order of the dimensions and padded
+    for strides in ((T * H * D, H * D, D), (D, B * H * D, B * D), (H * D, B * H * D, D), (T * D, D, B * T * D),
+                    (T * H * 80, H * 80, 80)):
+        out = room.as_strided(q.shape, strides + (1,))
+        r.apply(q, None, pos, out)
+        check(out, *oracle(q, pos, {}, D, "half", None, 0), torch.float16)
