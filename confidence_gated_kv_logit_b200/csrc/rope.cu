@@ -486,10 +486,13 @@ confkv_status confkv_rope(const confkv_rope_table* table, int32_t batch, int32_t
   std::memset(&a, 0, sizeof(a));
   const bool half = table->layout == CONFKV_ROPE_HALF;
   bool vec = (D == 32 || D == 64 || D == 128 || D == 256) && (!half || rd % 16 == 0);
-  const confkv_rope_rows* in[2] = {q, k};
   for (int sd = 0; sd < 2; ++sd) {
-    const confkv_rope_rows* r = in[sd];
-    if (!r) continue;
+    if (sd == 1 && !k) continue;
+    confkv_rope_rows own = sd ? *k : *q, *r = &own;
+    // a dimension of size 1 has no stride, whatever it says
+    if (batch == 1) r->x_batch = r->y_batch = 0;
+    if (tokens == 1) r->x_token = r->y_token = 0;
+    if (r->heads == 1) r->x_head = r->y_head = 0;
     if (r->heads < 1 || r->heads > (1 << 24) || !r->x || !r->y) return CONFKV_ERR_ARG;
     const uintptr_t px = reinterpret_cast<uintptr_t>(r->x), py = reinterpret_cast<uintptr_t>(r->y);
     const uintptr_t pw = reinterpret_cast<uintptr_t>(r->weight);
@@ -498,7 +501,7 @@ confkv_status confkv_rope(const confkv_rope_table* table, int32_t batch, int32_t
       return CONFKV_ERR_ARG;
     // distinct rows must be written to distinct places, those of q and k among them
     if (!rows_apart(D, batch, r->y_batch, tokens, r->y_token, r->heads, r->y_head)) return CONFKV_ERR_ARG;
-    if (sd == 1 && r->y == in[0]->y) return CONFKV_ERR_ARG;
+    if (sd == 1 && r->y == q->y) return CONFKV_ERR_ARG;
     if (px == py && (x_type != y_type || r->x_batch != r->y_batch || r->x_token != r->y_token || r->x_head != r->y_head))
       return CONFKV_ERR_ARG;
     const long long ex = 16 / (long long)xs, ey = 16 / (long long)ys;

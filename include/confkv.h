@@ -411,8 +411,8 @@ typedef struct {
 
 /* The rows of one side (queries, or keys): [batch][tokens][heads][head_dim]
  * with the last dimension contiguous and the other strides given in elements
- * (not negative; a column block of a packed projection, or a
- * [batch][heads][tokens][head_dim] buffer, are such rows). Rows of y lie apart:
+ * (not negative; that of a dimension of size 1 is not looked at; a column block of
+ * a packed projection, or a [batch][heads][tokens][head_dim] buffer, are such rows). Rows of y lie apart:
  * in the order of their strides, each dimension steps over all that the ones
  * before it span (ARG otherwise). y may be x itself with the same type and
  * strides; any other overlap, of the two sides' y among them, is not allowed. */

@@ -235,3 +235,19 @@ def test_outputs_whose_rows_overlap_are_refused():
         out = room.as_strided(q.shape, strides + (1,))
         r.apply(q, None, pos, out)
         check(out, *oracle(q, pos, {}, D, "half", None, 0), torch.float16)
+
+
+def test_dimensions_of_one_have_no_stride():
+    """Whatever stride a dimension of size 1 reports, the rows are the same: in place, and as an output."""
+    g = torch.Generator(device="cuda").manual_seed(10)
+    D, T = 64, 5
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)[None]
+    r = Rope(D)
+    q = make(1, T, 1, D, torch.float16, g)
+    want = torch.empty_like(q)
+    r.apply(q, None, pos, want)
+    out = torch.zeros_like(q)
+    r.apply(q.as_strided(q.shape, (7, D, 3, 1)), None, pos, out.as_strided(q.shape, (0, D, 1, 1)))
+    assert torch.equal(out, want)
+    r.apply(q.as_strided(q.shape, (7, D, 3, 1)), None, pos, q)
+    assert torch.equal(q, want)
