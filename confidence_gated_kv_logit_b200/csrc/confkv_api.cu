@@ -18,7 +18,7 @@ namespace {
 
 constexpr uint32_t kMagic = 0xC0F1C0DEu;
 constexpr uint32_t kDead = 0xDEADC0DEu;
-// Rows of split partials of tree attention: two waves of 256-row units (39 MB at head_dim 128).
+// Most rows of split partials of tree attention: two waves of 256-row units (39 MB at head_dim 128).
 constexpr long long kTreePartRows = 2 * 148 * 256;
 constexpr int kMaxCpr = 128;   // CTAs per logit row (one per ~4096 logits)
 
@@ -74,9 +74,9 @@ struct confkv_handle {
   unsigned* tickets;             // [Bmax]
   float* lse_ws;
   float* scores;
-  float* part;
-  int part_units;
-  float* tree_part;               // split partials of tree attention, kTreePartRows rows
+  float* part;                    // split partials of decode attention, or of tree attention (a call uses them up)
+  int part_units;                 // (item, split) units of decode attention
+  long long tree_part_rows;       // rows of tree attention
   uint32_t* vmask;
   int mask_words;
   unsigned char* qfrag;          // [S][qf_stride] query operands of the attention kernel
@@ -326,8 +326,10 @@ confkv_status confkv_create(int32_t layers, int32_t kv_heads, int32_t q_heads, i
   h->score_stride = c.cap + c.Wst;
   chk(B.alloc(&h->scores, S * G * (size_t)h->score_stride));
   h->part_units = (int)std::max<size_t>(std::min<size_t>(S * 8, 65536), 4096);
-  chk(B.alloc(&h->part, (size_t)h->part_units * G * (head_dim + 2)));
-  chk(B.alloc(&h->tree_part, (size_t)kTreePartRows * (head_dim + 2)));
+  // tree attention needs no more rows than every row of every segment in as many splits as there are tiles
+  const long long tiles = (c.cap + 63) / 64 + c.Wst / 64 + 1;
+  h->tree_part_rows = std::min<long long>(kTreePartRows, (long long)S * CONFKV_MAX_NODES * G * tiles);
+  chk(B.alloc(&h->part, (size_t)std::max<long long>((long long)h->part_units * G, h->tree_part_rows) * (head_dim + 2)));
   h->mask_words = (c.cap + 31) / 32;
   chk(B.alloc(&h->vmask, S * (size_t)h->mask_words));
   h->qf_stride = confkv::qfrag_bytes(head_dim, G);
@@ -643,8 +645,8 @@ confkv_status confkv_tree_attn(confkv_handle* h, int32_t layer, int32_t nodes, c
   a.score_stride = h->score_stride;
   a.max_cold_tokens = (int)std::min<long long>(ub, h->c.cap);
   a.num_sms = h->num_sms;
-  a.part = h->tree_part;
-  a.part_rows = kTreePartRows;
+  a.part = h->part;
+  a.part_rows = h->tree_part_rows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   h->conf_last = false;
   // a pass still deferred over these layers reads the scores that a tracked root overwrites

@@ -755,3 +755,12 @@ def test_eviction_right_after_a_tracked_tree(single, compact, N):
     assert all(h.last_error() == 0 for h in hs)
     for h in hs:
         h.close()
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 1), (128, 8)])
+def test_a_small_handle_stays_small(D, G):
+    """Tree attention's partials share decode attention's buffer, and a handle whose caches need few holds few."""
+    h = ConfKV(1, 1, G, D, n_low=32, n_high=64, max_prefill=60)
+    # decode attention's 4096 units; the cache, its scratch and its metadata are below 4 MB
+    assert h.query()["bytes_capacity"] <= 4096 * G * (D + 2) * 4 + (4 << 20)
+    h.close()
