@@ -433,12 +433,9 @@ confkv_status confkv_rope_prepare(const confkv_rope_params* p, confkv_rope_table
   if (p->scaling == CONFKV_ROPE_YARN &&
       !(finite_pos(p->beta_fast) && finite_pos(p->beta_slow) && p->beta_fast >= p->beta_slow))
     return CONFKV_ERR_ARG;
-  std::memset(out, 0, sizeof(*out));
-  out->head_dim = D;
-  out->rotary_dim = rd;
-  out->layout = p->layout;
   double theta = p->theta, mag = 1.0;
   if (p->scaling == CONFKV_ROPE_NTK && rd > 2) theta *= std::pow(p->factor, (double)rd / (rd - 2));
+  if (!std::isfinite(theta)) return CONFKV_ERR_ARG;
   double first = 0.0, last = 0.0;
   if (p->scaling == CONFKV_ROPE_YARN) {
     // the pair that makes `turns` turns within the original length
@@ -450,6 +447,11 @@ confkv_status confkv_rope_prepare(const confkv_rope_params* p, confkv_rope_table
     mag = 0.1 * std::log(p->factor) + 1.0;
   }
   if (p->magnitude > 0.0) mag = p->magnitude;
+  if (!finite_pos((float)mag)) return CONFKV_ERR_ARG;   // as the table holds it
+  std::memset(out, 0, sizeof(*out));
+  out->head_dim = D;
+  out->rotary_dim = rd;
+  out->layout = p->layout;
   out->magnitude = (float)mag;
   for (int i = 0; i < rd / 2; ++i) {
     double f = std::pow(theta, -2.0 * i / rd);   // radians a position

@@ -141,3 +141,14 @@ def test_calls_are_checked_on_the_host():
     broken = binding.RopeTable.from_buffer_copy(t)
     broken.rotary_dim = 300
     assert call(table=broken) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(magnitude=1e39), dict(magnitude=1e-60), dict(scaling="ntk", factor=1e300),
+                                dict(scaling="ntk", factor=1e200, theta=1e200)])
+def test_parameters_beyond_what_a_table_holds_are_refused(kw):
+    """A factor that is inf or 0 in fp32, and a base beyond fp64, would turn every value into inf, 0 or itself."""
+    with pytest.raises(binding.ConfKVError) as e:
+        binding.Rope(128, **kw)
+    assert e.value.status == 1
+    binding.Rope(128, magnitude=1e38)
+    binding.Rope(128, scaling="ntk", factor=1e100)
