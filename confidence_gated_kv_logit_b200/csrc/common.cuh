@@ -151,7 +151,7 @@ constexpr bool kChecked = false;
 
 // Check sites (value of err[1]).
 enum Site {
-  kSiteAppendSeg = 101, kSiteAppendSlot = 102, kSiteAppendCount = 103, kSiteAppendRow = 104,
+  kSiteAppendSeg = 101, kSiteAppendSlot = 102, kSiteAppendCount = 103, kSiteAppendRow = 104, kSiteAppendRoom = 105,
   kSiteAttnSeg = 201, kSiteAttnTile = 202, kSiteAttnScore = 203, kSiteAttnOut = 204, kSiteAttnQ = 205,
   kSiteTreeSeg = 206, kSiteTreeCount = 207,
   kSiteEmaSeg = 301, kSiteEmaCol = 302,

@@ -636,6 +636,20 @@ __global__ void __launch_bounds__(128) append_rows_kernel(const Cache c, const P
     ok = ok && row >= 0 && row < a.rows;
   }
   if (!__all_sync(0xffffffffu, ok)) return;
+  // nor of one that does not fit (the host's bound does not follow replays of a graph)
+  if (n_cold + n > c.cap) {
+    int cold = n;            // rows that the list adds outside the window
+    if (c.W > 0) {
+      // the window's tokens that reach age W on the way, and the list's own
+      cold = 0;
+      for (int sl = lane; sl < c.W; sl += 32) {
+        const int pos = c.pos_r[(size_t)s * c.Wst + sl];
+        cold += pos >= 0 && pos < t + n - c.W;
+      }
+      cold = __reduce_add_sync(0xffffffffu, cold) + max(0, n - c.W);
+    }
+    if (!guard(n_cold + cold <= c.cap, c.err, kSiteAppendRoom, s, n)) return;
+  }
   for (int i = 0; i < n; ++i) {
     const int row = a.index ? a.index[(size_t)b * a.tokens + i] : i;
     const size_t in_row = ((size_t)seq * a.rows + row) * c.Hkv + h;

@@ -262,7 +262,8 @@ CONFKV_API confkv_status confkv_tree_attn(confkv_handle* h, int32_t layer, int32
  *          (NULL: 0, 1, ...; then tokens must not exceed rows)
  *   counts int32 [batch], device, optional: tokens of each sequence, 0..tokens
  *          (NULL: tokens)
- * A count or row out of range sets the device word (ERR_DEVICE) and that
+ * A count or row out of range, or a list that a full cache has no room for (in
+ * replays of a captured call), sets the device word (ERR_DEVICE) and that
  * sequence gets none of its tokens. CAPACITY if `tokens` more could overflow
  * the cache: in confidence mode size max_prefill for the longest draft beyond
  * the budget; a fixed-budget cache has room for CONFKV_MAX_NODES beyond its own. */

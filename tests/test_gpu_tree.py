@@ -764,3 +764,34 @@ def test_a_small_handle_stays_small(D, G):
     # decode attention's 4096 units; the cache, its scratch and its metadata are below 4 MB
     assert h.query()["bytes_capacity"] <= 4096 * G * (D + 2) * 4 + (4 << 20)
     h.close()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(compact=2), dict(int8_enable=0), dict(W=1), dict(W=30)],
+                         ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()) or "default")
+def test_a_full_cache_takes_none_of_a_list(kw):
+    """Replays of a captured append go on past the host's bound: a sequence whose list no longer fits gets none of
+    it (not the part that would), sets the device word, and the other goes on."""
+    g = synth.generator(47, "cuda")
+    n = 20
+    h = build_handle(2, 4, 64, [100, 10], g, **dict(dict(W=16, single_stream=1, n_low=32, n_high=32, max_prefill=100), **kw))
+    W = 0 if kw.get("int8_enable") == 0 else kw.get("W", 16)
+    _, kd, vd = drafts((2,), n, 4, 2, 64, g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h.append(kd, vd, layer=0)
+    lens, cap, refused = [100, 10], 128, 0
+    for _ in range(4):
+        before = [logical_segment(h.export_segment(0, b, kv)) for b in range(2) for kv in range(2)]
+        graph.replay()
+        torch.cuda.synchronize()
+        fits = [x + n - W <= cap for x in lens]       # rows outside the window
+        refused += not all(fits)
+        assert h.last_error(clear=True) == (0 if all(fits) else 7)
+        lens = [x + n if f else x for x, f in zip(lens, fits)]
+        for i, was in enumerate(before):
+            now = logical_segment(h.export_segment(0, i // 2, i % 2))
+            assert len(now["pos"]) == now["next_pos"] == lens[i // 2]
+            if not fits[i // 2]:
+                assert all(np.array_equal(was[key], now[key]) for key in was)
+    assert refused
+    h.close()
