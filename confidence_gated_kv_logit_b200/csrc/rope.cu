@@ -9,10 +9,11 @@
 // and (2i, 2i + 1) in the interleaved one; m is the scaling's magnitude factor.
 //
 // Angles. f_i is kept as a fraction of a turn a position in 64-bit fixed point,
-// F_i = f_i / (2 pi) * 2^64 mod 2^64. The product pos * F_i mod 2^64 is then the
-// angle modulo one turn with an error of |pos| * 2^-63 turns, exact enough for
-// every 32-bit position, where a 32-bit float product would be off by a radian
-// from positions of a few million on. Its top 32 bits go to sincospif.
+// F_i = f_i / (2 pi) * 2^64 mod 2^64, right to 2^-55 of a turn (f_i comes from
+// fp64). The product pos * F_i mod 2^64 is then the angle modulo one turn, off by
+// |pos| * 2^-55 turns, 2^-24 at the last 32-bit position, where a 32-bit float
+// product would be off by a radian from positions of a few million on. Its top 32
+// bits go to sincospif as a float, which rounds them to 2^-26 of a turn.
 //
 // The kernel reads and writes every value once and is bound by HBM; the sines of
 // a token are computed once per warp and used for every head that the warp

@@ -34,10 +34,10 @@
 // Sums over a gathered list are units of 2^-40 of the largest. The exponent
 // (x - max) / (T ln 2) carries a correction for its rounding, which alone would move
 // the weights of far tokens by 1e-6.
-// Measured: 16 rows of 128256 fp32 with top-k 1000, top-p and min-p 31 us, 256 rows
-// with top-p 0.9 200 us (0.66 TB/s: the dozen barriers between a row's phases bound
+// Measured: 16 rows of 128256 fp32 with top-k 1000, top-p and min-p 30 us, 256 rows
+// with top-p 0.9 206 us (0.64 TB/s: the dozen barriers between a row's phases bound
 // it, with 37% of the issue slots used), 33 bf16 rows of 152064 with min-p
-// 13 us, one row of 50257 with top-k and top-p 13 us, all latency.
+// 14 us, one row of 50257 with top-k and top-p 13 us, all latency.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>

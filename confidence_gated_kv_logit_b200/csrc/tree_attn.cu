@@ -16,10 +16,11 @@
 //   * INT8 codes are widened to fp16 in registers (exact), straight from the
 //     shared-memory tile; scores get the K scale in fp32, probabilities the V
 //     scale, so the codes themselves are never rounded.
-//   * P = p * vs is split into two fp16 parts (22 bits), relative to a power of
-//     two near the largest V scale and to a running maximum that is moved only
-//     when a score passes it by 2^8. One part alone would add an error as large
-//     as the output's own rounding to fp16, and more where a few keys dominate.
+//   * P = p * vs is split into two fp16 parts (22 bits, down to fp16's smallest
+//     step), relative to a power of two near the largest V scale and to a running
+//     maximum that is moved only when a score passes it by 2^8. One part alone would
+//     add an error as large as the output's own rounding to fp16, and more where a
+//     few keys dominate.
 // The token order within a tile is permuted so that one 32-bit word of V codes
 // (four tokens of one dimension) is the B operand of a k-step as it lies: column
 // c of the score block 2j + e holds token 16 j + 4 (c / 2) + 2 e + (c % 2).
@@ -41,7 +42,11 @@ namespace confkv {
 namespace {
 
 constexpr int kMaxWarps = 8;       // consumer warps
-constexpr int kMaxRows = 32;       // rows per KV head of this kernel; more go to the one of tree_mma.cu
+// Rows per KV head of this kernel; more go to the one of tree_mma.cu. Cold, for 32/8
+// heads of 128, this kernel against that one: 8 rows over 16384 tokens x 2 sequences
+// 48 and 60 us, over 2048 x 16 56 and 63, over 512 x 16 36 and 33; 32 rows 63 and 65,
+// 67 and 65, 39 and 35.
+constexpr int kMaxRows = 32;
 
 template <int D, bool CI8>
 struct TCfg {

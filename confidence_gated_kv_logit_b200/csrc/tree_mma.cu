@@ -645,7 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_mma_kernel(const Cache c, co
             ls1 = __fadd2_rn(ls1, q);
             p = __fmul2_rn(p, make_float2(vs.x, vs.y));
             q = __fmul2_rn(q, make_float2(vs.z, vs.w));
-            // high part: the mantissa cut to fp16's ten bits (exact in fp16); low part: what that leaves
+            // high part: the mantissa cut to fp16's ten bits (exact in fp16 from 2^-14 up; below, fp16's smallest
+            // step bounds both parts); low part: what that leaves
             const float2 ph = pair(__float_as_uint(p.x) & 0xffffe000u, __float_as_uint(p.y) & 0xffffe000u);
             const float2 qh = pair(__float_as_uint(q.x) & 0xffffe000u, __float_as_uint(q.y) & 0xffffe000u);
             const float2 pl = __fadd2_rn(p, make_float2(-ph.x, -ph.y)), ql = __fadd2_rn(q, make_float2(-qh.x, -qh.y));

@@ -238,10 +238,12 @@ CONFKV_API confkv_status confkv_decode_attn(confkv_handle* h, int32_t layer, con
  *          confkv_decode_attn does with its token's; a sequence without nodes
  *          gives mass 0. Confidence mode only (ARG in fixed mode)
  * A node that attends to nothing (an empty cache and an empty mask) gets out 0
- * and lse -inf. Scores and sums are fp32 and the weights of the second product
- * keep 22 bits; the output's rounding to fp16 is the only one below that. Keys
- * and values of a node reach only the nodes that attend to it, whatever they
- * are (NaN, inf).
+ * and lse -inf. Scores and sums are fp32. The weights of the second product
+ * (relative to the largest, and times the V scale for INT8 rows) keep 22 bits, down
+ * to steps of 2^-31 max(1, the largest V scale of the cache): beside a V row 2^20
+ * times the others, at a scale of 1, those keep 11 bits. The output's rounding to
+ * fp16 is the only other one below fp32. Keys and values of a node reach only the
+ * nodes that attend to it, whatever they are (NaN, inf).
  * Errors: STATE before prefill or with another device current. */
 enum { CONFKV_MAX_NODES = 64 };
 CONFKV_API confkv_status confkv_tree_attn(confkv_handle* h, int32_t layer, int32_t nodes, const void* q, const void* k,
@@ -437,7 +439,8 @@ CONFKV_API confkv_status confkv_rope_prepare(const confkv_rope_params* params, c
  *   positions  int32 [batch][tokens], device; any value (a negative position
  *              turns backwards)
  *   x_type, y_type  CONFKV_F32, CONFKV_F16 or CONFKV_BF16, the same for q and k
- * Arithmetic is fp32 with angles exact to 2^-32 of a turn; the output type's
+ * Arithmetic is fp32. Angles are right to 2^-26 of a turn, and |position| * 2^-55
+ * of one for the frequencies, which are prepared in fp64. The output type's
  * rounding is the only one below fp32. batch or tokens of 0 does nothing. */
 CONFKV_API confkv_status confkv_rope(const confkv_rope_table* table, int32_t batch, int32_t tokens,
                                      const int32_t* positions, int32_t x_type, int32_t y_type, float eps,
@@ -472,7 +475,7 @@ CONFKV_API confkv_status confkv_rope(const confkv_rope_table* table, int32_t bat
  * are fp64 over fours added in fp32, or integers: for the top_p cut of 2^-30 of each weight's own
  * magnitude and 2^-32 of the largest weight over the whole row, over up to 2048 gathered tokens
  * of 2^-40 of the largest. None depends on timing: a call repeated gives the same bits.
- * CAPACITY: vocab above 1048576. rows of 0 does nothing. */
+ * CAPACITY: vocab above 1048576, or rows above 2^27. rows of 0 does nothing. */
 CONFKV_API confkv_status confkv_sample(int32_t type, const void* logits, int64_t row_stride, int32_t rows,
                                        int32_t vocab, const float* u, const float* temperature, const int32_t* top_k,
                                        const float* top_p, const float* min_p, int32_t* token_out, float* prob_out,
