@@ -251,3 +251,21 @@ def test_dimensions_of_one_have_no_stride():
     assert torch.equal(out, want)
     r.apply(q.as_strided(q.shape, (7, D, 3, 1)), None, pos, q)
     assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("x", list(TYPES))
+@pytest.mark.parametrize("y", list(TYPES))
+@pytest.mark.parametrize("D,rd,layout", [(128, 128, "half"), (64, 64, "interleaved"), (128, 102, "half"), (96, 96, "interleaved")])
+def test_every_pair_of_types(x, y, D, rd, layout):
+    g = torch.Generator(device="cuda").manual_seed(11)
+    B, T, Hq, Hk = 2, 3, 5, 2
+    q, k = make(B, T, Hq, D, TYPES[x], g), make(B, T, Hk, D, TYPES[x], g)
+    pos = torch.randint(0, 100000, (B, T), generator=g, device="cuda", dtype=torch.int32)
+    w = 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    r = Rope(D, rotary_dim=rd, layout=layout)
+    for qw in (None, w):
+        qo = torch.full((B, T, Hq, D), 7.0, dtype=TYPES[y], device="cuda")
+        ko = torch.full((B, Hk, T, D), 7.0, dtype=TYPES[y], device="cuda")
+        r.apply(q, k, pos, qo, ko.transpose(1, 2), q_weight=qw, k_weight=w)
+        check(qo, *oracle(q, pos, {}, rd, layout, qw, 1e-6), TYPES[y])
+        check(ko.transpose(1, 2), *oracle(k, pos, {}, rd, layout, w, 1e-6), TYPES[y])

@@ -795,3 +795,60 @@ def test_a_full_cache_takes_none_of_a_list(kw):
                 assert all(np.array_equal(was[key], now[key]) for key in was)
     assert refused
     h.close()
+
+
+@pytest.mark.parametrize("N,Hq", [(3, 4), (40, 8)])
+def test_fewer_sequences_than_the_handle_is_sized_for(N, Hq):
+    """Three sequences in a handle of five, every layer in one call: drafts, roots and appends as in a handle of three."""
+    L, B, Hkv, D, lens = 2, 3, 2, 64, [200, 31, 90]
+    hs = [build_handle(Hkv, Hq, D, lens, synth.generator(50, "cuda"), L=L, decode=3, max_batch=m) for m in (3, 5)]
+    g = synth.generator(51, "cuda")
+    q, kd, vd = drafts((L, B), N, Hq, Hkv, D, g)
+    mask = dev_mask(tree_masks(B, N, np.random.RandomState(6)))
+    counts = torch.tensor([N, 1, N - 1], dtype=torch.int32, device="cuda")
+    index = torch.tensor([[0, N - 1], [0, 0], [1, 0]], dtype=torch.int32, device="cuda")
+    outs = []
+    for h in hs:
+        outs.append((torch.full_like(q, 7.0), torch.full((L, B, N, Hq), 7.0, device="cuda")))
+        h.tree_attn(q, kd, vd, mask, outs[-1][0], counts=counts, lse_out=outs[-1][1], track=True)
+        h.append(kd, vd, index=index, counts=torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda"))
+        h.evict_compact()
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    for l in range(L):
+        for b in range(B):
+            for kv in range(Hkv):
+                x, y = (logical_segment(h.export_segment(l, b, kv)) for h in hs)
+                assert all(np.array_equal(x[key], y[key]) for key in x)
+    assert all(h.last_error() == 0 for h in hs)
+    for h in hs:
+        h.close()
+
+
+@pytest.mark.parametrize("N,Hq", [(6, 8), (20, 8), (64, 16)])
+def test_queries_that_are_not_finite_stay_in_their_rows(N, Hq):
+    g = synth.generator(52, "cuda")
+    lens = [300, 20]
+    h = build_handle(2, Hq, 128, lens, g)
+    q, kd, vd = drafts((2,), N, Hq, 2, 128, g)
+    masks = tree_masks(2, N, np.random.RandomState(7))
+    q2 = q.clone()
+    q2[0, 1, 0] = math.nan
+    q2[1, 4, Hq - 1, 3] = math.inf
+    out, lse = torch.full_like(q, 7.0), torch.full((2, N, Hq), 7.0, device="cuda")
+    h.tree_attn(q2, kd, vd, dev_mask(masks), out, 0, lse_out=lse)
+    assert torch.isnan(out[0, 1, 0]).all() and torch.isnan(lse[0, 1, 0])
+    assert torch.isnan(out[1, 4, Hq - 1]).all()
+    # the others, by the rows of the same call with zeros in those two places
+    q2[0, 1, 0] = 0
+    q2[1, 4, Hq - 1, 3] = 0
+    clean, clean_lse = torch.full_like(q, 7.0), torch.full_like(lse, 7.0)
+    h.tree_attn(q2, kd, vd, dev_mask(masks), clean, 0, lse_out=clean_lse)
+    for b in range(2):
+        for kv in range(2):
+            check_segment(h, clean, clean_lse, q2, kd, vd, masks, [N, N], 0, b, kv)
+    out[0, 1, 0], lse[0, 1, 0] = clean[0, 1, 0], clean_lse[0, 1, 0]
+    out[1, 4, Hq - 1], lse[1, 4, Hq - 1] = clean[1, 4, Hq - 1], clean_lse[1, 4, Hq - 1]
+    for b in range(2):
+        for kv in range(2):
+            check_segment(h, out, lse, q2, kd, vd, masks, [N, N], 0, b, kv)
+    h.close()
